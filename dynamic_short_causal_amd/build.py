@@ -4,7 +4,8 @@ Every source is compiled for gfx950 only.  Packed-fp32 instruction selection
 is switched off for all device code.  Objects go to ``_build/`` at the
 repository root; the library lands next to this file.  The compiler's
 per-kernel resource report is kept in ``_build/kernel_resources.txt`` and the
-build fails if any kernel spills registers to scratch memory.
+build fails if any kernel spills registers to scratch memory.  A build that
+fails leaves no ``libdsc.so``: an older one would pass for its result.
 """
 import concurrent.futures as cf
 import os
@@ -74,8 +75,24 @@ def _resources(remarks):
     return rows
 
 
+# The generic low-rank backward for 33..64 ranks (RB = 4, the last template
+# argument) keeps the filter fragments of all four rank blocks resident; its
+# widest instance (bf16, H = 1, W = 8, packed rows) needs a little scratch.
+# That path is correct and untuned; every other kernel must not spill.
+MAY_SPILL = re.compile(r"lr_bwd_kernelI.*ELi4EEEv")
+
+
+def _refuse_spills(rows):
+    spills = [r["name"] for r in rows if r.get("ScratchSize [bytes/lane]", "0") != "0"
+              and not MAY_SPILL.search(r["name"])]
+    if spills:
+        raise RuntimeError(f"{len(spills)} kernels spill to scratch, e.g. {spills[:3]}")
+
+
 def build(jobs=None):
     """Compile every source and link ``libdsc.so``; returns the library path."""
+    if os.path.exists(LIB):
+        os.remove(LIB)
     os.makedirs(OBJ, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, min(16, os.cpu_count() or 2)))
     with cf.ThreadPoolExecutor(jobs) as ex:
@@ -89,15 +106,7 @@ def build(jobs=None):
             f.write(f"{r['name']} vgpr={r.get('VGPRs')} agpr={r.get('AGPRs')} "
                     f"scratch={r.get('ScratchSize [bytes/lane]')} "
                     f"waves_per_simd={r.get('Occupancy [waves/SIMD]')}\n")
-    # The generic low-rank backward for 33..64 ranks (RB = 4, the last template
-    # argument) keeps the filter fragments of all four rank blocks resident; its
-    # widest instance (bf16, H = 1, W = 8, packed rows) needs a little scratch.
-    # That path is correct and untuned; every other kernel must not spill.
-    may_spill = re.compile(r"lr_bwd_kernelI.*ELi4EEEv")
-    spills = [r["name"] for r in rows if r.get("ScratchSize [bytes/lane]", "0") != "0"
-              and not may_spill.search(r["name"])]
-    if spills:
-        raise RuntimeError(f"{len(spills)} kernels spill to scratch, e.g. {spills[:3]}")
+    _refuse_spills(rows)
     objs = [o for o, _, _ in results]
     tmp = LIB + ".tmp"
     subprocess.run([HIPCC, "-shared", "--offload-arch=gfx950", "-fPIC", *objs, "-o", tmp],

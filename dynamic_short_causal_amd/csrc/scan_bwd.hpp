@@ -316,12 +316,27 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_sums_kernel(ScanBwdP p) {
 // ---------------------------------------------------------------------------
 // main
 // ---------------------------------------------------------------------------
-// Two workgroups of four waves a CU, that is 256 registers a wave, even where 60
-// to 100 bytes of them go to memory for it: 8 x 2048 x 1536, N = 16, fp32 takes
-// 733 us so and 981 us with one workgroup, bf16 with eight taps 817 and 1095
-// us.  fp32 with eight taps would lose 260 bytes, and 1517 against 1346 us.
+// Two workgroups of four waves a CU, that is 256 registers a wave: 8 x 2048 x
+// 1536, N = 16, fp32 takes 684 us so and 932 us with one workgroup, bf16 with
+// eight taps 733 and 1031 us.  fp32 with eight taps does not fit: 1110 us with
+// the rest in memory, 1052 us with one workgroup.
 constexpr int scan_bwd_occupancy(int esize, int nw, int wm) {
   return nw == 4 && (esize == 2 || wm <= 4) ? 2 : 1;
+}
+// Those that fit only without the addresses and values that can be had again
+// where they are used.  The compiler would put 60 to 100 bytes a lane into memory
+// instead: 711 and 768 us for the two above.  bf16 with four taps has room for
+// all: 1272 us at 8 x 4096 x 1536, 1301 us without them.
+constexpr bool scan_bwd_tight(int esize, int nw, int wm) {
+  return scan_bwd_occupancy(esize, nw, wm) == 2 && (esize == 4 || wm > 4);
+}
+
+// v, where tight as a value that the compiler does not know to be the same in
+// every tile: it forms the addresses that depend on it where they are used,
+// instead of keeping them in registers (two an address) through the recurrences.
+template <bool TIGHT> __device__ __forceinline__ int in_loop(int v) {
+  if constexpr (TIGHT) asm volatile("" : "+v"(v));
+  return v;
 }
 
 template <typename E, int NS, int NW, int WM, bool PACKED>
@@ -332,6 +347,7 @@ __global__ __launch_bounds__(64 * NW)
   constexpr int TT = Geo::TT, Np = Geo::Np, PV = Geo::PV, NI = Geo::NI;
   constexpr int NV = Geo::NV, NR = Geo::NR, BR = 2 * NS * NW;
   constexpr int HALO = kScanMaxW - 1, KA = 3 + WM;
+  constexpr bool TIGHT = scan_bwd_tight(sizeof(E), NW, WM);
   __shared__ __align__(16) E s_w[WM][kScanCh];
   __shared__ __align__(16) float s_par[3][kScanCh];
   __shared__ __align__(16) float s_dt[TT][kScanCh], s_du[TT][kScanCh], s_dp[TT][kScanCh];
@@ -378,7 +394,6 @@ __global__ __launch_bounds__(64 * NW)
   }
   const int v0 = (int)threadIdx.x % NV * PV, r0 = (int)threadIdx.x / NV * NI;
   const bool prep = r0 < TT && v0 < at.nch;
-  const int64_t cv = at.c0 + v0;
   // sums over the thread's tokens for dDk, ddt_bias, dcb and dw
   float acc[KA][PV];
 #pragma unroll
@@ -403,13 +418,14 @@ __global__ __launch_bounds__(64 * NW)
   const ScanOff off = scan_off(a, r0, v0);
   float hn[NS], cumn = 0.0f;  // the tile's start as the sums kernel left it
   auto ahead = [&](int t) {
-    ld_bc<E, NS, NW, TT>(a, at.b, at.g, t, t1, bcr);
-    const int64_t row = ((int64_t)at.b * p.tiles + t / TT) * a.D + c;
+    ld_bc<E, NS, NW, TT>(a, at.b, at.g, t, t1, bcr, in_loop<TIGHT>((int)threadIdx.x));
+    const int64_t row = ((int64_t)at.b * p.tiles + t / TT) * a.D + in_loop<TIGHT>((int)c);
     ld_lds<NS>(p.ws.ck + row * Np + n0, hn);
     if (p.nc > 1) cumn = p.ws.cum[row];
     if (prep) {
-      ld_tile<E, PV, NI, WM, TT>(a, at.b, t, r0, t1, at.c0, v0, off, gate, nxt);
-      ld_dy<E, PV, NI>(a, at.b, t, r0, t1, at.c0, off, dyn);
+      const int ro = in_loop<TIGHT>(r0), vo = in_loop<TIGHT>(v0);
+      ld_tile<E, PV, NI, WM, TT>(a, at.b, t, ro, t1, at.c0, vo, off, gate, nxt);
+      ld_dy<E, PV, NI>(a, at.b, t, ro, t1, at.c0, off, dyn);
     }
   };
   ahead(t0 + (nt - 1) * TT);
@@ -534,6 +550,10 @@ __global__ __launch_bounds__(64 * NW)
         }
         const bool on = t + r0 + i < t1;
         const int64_t n = (tokn + i) * a.D + at.c0;
+        if constexpr (TIGHT) {
+          ld_lds<PV>(&s_dt[r0 + i][v0], k.dt[i]);
+          ld_lds<PV>(&s_dp[r0 + i][v0], k.dp[i]);
+        }
         float ddelta[PV];
 #pragma unroll
         for (int j = 0; j < PV; ++j) {
@@ -603,6 +623,7 @@ __global__ __launch_bounds__(64 * NW)
         }
         const int from_end = t1 - 1 - tt;
         const int64_t edge = ((int64_t)at.b * p.nc + at.chunk) * HALO;
+        const int64_t cv = at.c0 + in_loop<TIGHT>(v0);
         if (t1 < T && from_end < a.W - 1)
           st_row<float, PV>(p.ws.tail + (edge + from_end) * a.D + cv, dx);
         else

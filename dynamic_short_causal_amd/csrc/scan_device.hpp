@@ -151,11 +151,11 @@ template <typename E, int NS, int NW, int TT, int TH = 64 * NW> struct BcRaw {
   RowBits<E, BcGeo<NS, NW, TT, TH>::QN> q[BcGeo<NS, NW, TT, TH>::NQ];
 };
 
-// Where run k of the thread goes: token, B or C, first state, place in LDS.
+// Where run k of thread tid goes: token, B or C, first state, place in LDS.
 template <int NS, int NW, int TT, int TH>
-__device__ __forceinline__ void bc_at(int k, int &row, int &which, int &n0, int &at) {
+__device__ __forceinline__ void bc_at(int tid, int k, int &row, int &which, int &n0, int &at) {
   typedef BcGeo<NS, NW, TT, TH> G;
-  at = ((int)threadIdx.x + k * TH) * G::QN;
+  at = (tid + k * TH) * G::QN;
   row = at / G::row;
   const int r = at % G::row, group = r / (2 * NS), i = r % (2 * NS);
   which = i / NS;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void bc_at(int k, int &row, int &which, int &n0, int 
 
 template <typename E, int NS, int NW, int TT, int TH = 64 * NW>
 __device__ __forceinline__ void ld_bc(const ScanArgs &a, int b, int g, int t, int t1,
-                                      BcRaw<E, NS, NW, TT, TH> &o) {
+                                      BcRaw<E, NS, NW, TT, TH> &o, int tid = (int)threadIdx.x) {
   typedef BcGeo<NS, NW, TT, TH> G;
 #pragma unroll
   for (int k = 0; k < G::NQ; ++k) {
@@ -172,7 +172,7 @@ __device__ __forceinline__ void ld_bc(const ScanArgs &a, int b, int g, int t, in
 #pragma unroll
     for (int i = 0; i < RowBits<E, G::QN>::dwords; ++i) r.d[i] = 0u;
     int row, which, n0, at;
-    bc_at<NS, NW, TT, TH>(k, row, which, n0, at);
+    bc_at<NS, NW, TT, TH>(tid, k, row, which, n0, at);
     if (t + row >= t1 || n0 >= a.N) continue;
     const int64_t tok = (int64_t)b * a.T + t + row;
     const E *p = (which ? (const E *)a.Cm + tok * a.c_row : (const E *)a.Bm + tok * a.b_row) +
@@ -196,7 +196,7 @@ __device__ __forceinline__ void st_bc(const BcRaw<E, NS, NW, TT, TH> &o, float *
 #pragma unroll
   for (int k = 0; k < G::NQ; ++k) {
     int row, which, n0, at;
-    bc_at<NS, NW, TT, TH>(k, row, which, n0, at);
+    bc_at<NS, NW, TT, TH>((int)threadIdx.x, k, row, which, n0, at);
     float v[G::QN];
     unpack_row<E, G::QN>(o.q[k], v);
     st_row<float, G::QN>(s_bc + at, v);
