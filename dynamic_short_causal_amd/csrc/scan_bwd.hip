@@ -1,6 +1,6 @@
 // scan_bwd.hip -- dispatch of the selective-scan backward (scan_bwd.hpp) and the
 // kernel that adds its partial sums.
-#include "scan_bwd.hpp"
+#include "scan_device.hpp"
 
 namespace dsc {
 
@@ -96,6 +96,7 @@ __global__ __launch_bounds__(kScanFinThreads) void scan_bwd_finish_kernel(ScanBw
   }
 }
 
+// instantiated in scan_bwd_{bf16,f32}.hip
 template <typename E, int NS, int NW> hipError_t scan_bwd_nw(const ScanBwdP &, int64_t);
 
 template <typename E> static hipError_t bwd(const ScanArgs &a) {

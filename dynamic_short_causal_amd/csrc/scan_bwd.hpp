@@ -44,21 +44,6 @@
 
 namespace dsc {
 
-// Workspace of a backward call, in floats.
-struct ScanBwdWs {
-  float *ck, *cum;          // tile starts: (B, tiles, D, Np), (B, tiles, D)
-  float *hend, *qend, *sdt; // chunks: (B, nc, D, Np) twice, (B, nc, D)
-  float *dbc;               // (G nblk, B T, 2 Np): dC then dB of a channel block
-  float *pA, *pV;           // (B nc, D, Np), (B nc, kScanParV, D)
-  float *tail, *head;       // (B nc, 7, D) twice: see the convolution's seam below
-};
-
-struct ScanBwdP {
-  ScanArgs a;
-  ScanBwdWs ws;
-  int dg, nblk, nc, tc, tiles;
-};
-
 // Shape of a workgroup: NW waves of NS states, tiles of TT tokens, of which a
 // thread prepares NI consecutive ones of PV channels.
 template <int NS_, int NW_> struct BwdGeo {

@@ -30,6 +30,22 @@ struct ScanP {
   int dg, nblk, nc, tc;
 };
 
+// Workspace of a backward call, in floats.
+struct ScanBwdWs {
+  float *ck, *cum;          // tile starts: (B, tiles, D, Np), (B, tiles, D)
+  float *hend, *qend, *sdt; // chunks: (B, nc, D, Np) twice, (B, nc, D)
+  float *dbc;               // (G nblk, B T, 2 Np): dC then dB of a channel block
+  float *pA, *pV;           // (B nc, D, Np), (B nc, kScanParV, D)
+  float *tail, *head;       // (B nc, 7, D) twice: see the convolution's seam below
+};
+
+// Parameters of the backward kernels.
+struct ScanBwdP {
+  ScanArgs a;
+  ScanBwdWs ws;
+  int dg, nblk, nc, tc, tiles;
+};
+
 // V consecutive floats of LDS, aligned to their size (16 bytes at most)
 template <int V>
 __device__ __forceinline__ void ld_lds(const float *p, float (&o)[V]) {

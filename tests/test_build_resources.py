@@ -43,3 +43,11 @@ def test_a_failed_build_leaves_no_library(builder, monkeypatch):
     with pytest.raises(RuntimeError):
         builder.build(jobs=1)
     assert not os.path.exists(builder.LIB)
+
+
+def test_the_scan_dispatch_holds_no_kernels_of_the_units(builder):
+    """scan_bwd.hip compiles its own kernel; the others come from the units that
+    are compiled once per number of waves, and once only."""
+    _, _, remarks = builder._compile(("scan_bwd.hip", ()))
+    names = [r["name"] for r in builder._resources(remarks)]
+    assert len(names) == 2 and all("scan_bwd_finish_kernel" in n for n in names), names
