@@ -260,23 +260,29 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_sums_kernel(ScanBwdP p) {
           g.dp[i] = CUT ? s_dp[CUT ? g0 + i : 0][lane] : 0.0f;
         }
       };
+      // the tile's tokens before the chunk's first start of a document
+      const int first = fresh ? 0 : starts ? __builtin_ctz(starts) : TT;
+      fresh |= starts != 0;
       auto walk = [&](int g0, const Group &g) {
 #pragma unroll
         for (int i = 0; i < GT; ++i) {
           const bool start = PACKED && (starts >> (g0 + i) & 1);
+          // nothing of a document that starts in the chunk goes to the tokens
+          // before the chunk: left out, since its values may be infinite
+          const bool before = !PACKED || g0 + i < first;
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
             const float e = __builtin_amdgcn_exp2f(g.dt[i] * A2[j]);
             h[j] = fmaf(e, start ? 0.0f : h[j], g.du[i] * g.bc[i][j]);
             if constexpr (CUT) {
-              pr[j] = start ? 0.0f : pr[j] * e;
-              qe[j] = fmaf(pr[j], g.dp[i] * g.bc[i][CUT ? NS + j : 0], qe[j]);
+              pr[j] *= e;
+              const float more = fmaf(pr[j], g.dp[i] * g.bc[i][CUT ? NS + j : 0], qe[j]);
+              qe[j] = before ? more : qe[j];
             }
           }
           cum += g.dt[i];
         }
       };
-      fresh |= starts != 0;
       load(0, gr[0]);
 #pragma unroll 1
       for (int g0 = 0; g0 < TT; g0 += 2 * GT) {
