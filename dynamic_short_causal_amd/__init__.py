@@ -7,9 +7,11 @@ is missing, importing this package raises.
 
 The functions named like the C entry points (``dsc_headwise_fwd`` ...) take
 pre-allocated output tensors; ``headwise_fwd`` and friends allocate them with
-``torch.empty`` and call the former.
+``torch.empty``, on the stream of the call, and call the former.
 """
 import ctypes
+import functools
+import inspect
 import math
 import os
 
@@ -531,15 +533,42 @@ def dsc_layernorm_bwd(x, w, dy, mean, rstd, dx, dw, db, workspace, stream=None):
 
 
 # --------------------------------------------------------------- allocating forms
+def _on_stream(call):
+    """An allocating form whose tensors belong to the stream that it is queued on.
+
+    Memory from the current stream's pool would go back to it as soon as a
+    workspace (or an output that the caller drops) is released, and to that
+    stream's next tensor while the kernels on the other stream still use it.
+    Outputs are recorded on the current stream too, where the caller reads them."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None or stream.cuda_stream == _stream(None):
+            return call(*args, **kwargs)
+        current = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = call(*args, **kwargs)
+        outs = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,)
+        for t in outs:
+            t.record_stream(current)
+        return out
+    return run
+
+
+@_on_stream
 def headwise_fwd(x, w, H, residual=False, act=False, stream=None):
     return dsc_headwise_fwd(x, w, torch.empty_like(x), H, residual, act, stream)
 
 
+@_on_stream
 def headwise_bwd(x, w, dy, H, residual=False, act=False, stream=None):
     return dsc_headwise_bwd(x, w, dy, torch.empty_like(x), torch.empty_like(w), H, residual,
                             act, stream)
 
 
+@_on_stream
 def lowrank_fwd(x, z, U, W, H, residual=False, act=False, stream=None):
     return dsc_lowrank_fwd(x, z, U, torch.empty_like(x), W, H, residual, act, stream)
 
@@ -550,6 +579,7 @@ def lowrank_workspace(x, z, W, H):
     return torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
 
 
+@_on_stream
 def lowrank_bwd(x, z, U, dy, W, H, residual=False, act=False, workspace=None, stream=None):
     if workspace is None:
         workspace = lowrank_workspace(x, z, W, H)
@@ -557,19 +587,23 @@ def lowrank_bwd(x, z, U, dy, W, H, residual=False, act=False, workspace=None, st
                            torch.empty_like(U), workspace, W, H, residual, act, stream)
 
 
+@_on_stream
 def decode_state(x, W, stream=None):
     B, T, D = x.shape
     return dsc_decode_state(x, torch.empty(B, W - 1, D, dtype=x.dtype, device=x.device), stream)
 
 
+@_on_stream
 def headwise_decode(x, w, state, H, residual=False, act=False, stream=None):
     return dsc_headwise_decode(x, w, state, torch.empty_like(x), H, residual, act, stream)
 
 
+@_on_stream
 def lowrank_decode(x, z, U, state, W, H, residual=False, act=False, stream=None):
     return dsc_lowrank_decode(x, z, U, state, torch.empty_like(x), W, H, residual, act, stream)
 
 
+@_on_stream
 def static_fwd(x, w, H, residual=False, act=False, stream=None):
     return dsc_static_fwd(x, w, torch.empty_like(x), H, residual, act, stream)
 
@@ -580,6 +614,7 @@ def static_workspace(x, W, H):
     return torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
 
 
+@_on_stream
 def static_bwd(x, w, dy, H, residual=False, act=False, workspace=None, stream=None):
     if workspace is None:
         workspace = static_workspace(x, w.shape[-1], H)
@@ -587,19 +622,23 @@ def static_bwd(x, w, dy, H, residual=False, act=False, workspace=None, stream=No
                           residual, act, stream)
 
 
+@_on_stream
 def headwise_fwd_varlen(x, w, pos, H, residual=False, act=False, stream=None):
     return dsc_headwise_fwd_varlen(x, w, pos, torch.empty_like(x), H, residual, act, stream)
 
 
+@_on_stream
 def headwise_bwd_varlen(x, w, pos, dy, H, residual=False, act=False, stream=None):
     return dsc_headwise_bwd_varlen(x, w, pos, dy, torch.empty_like(x), torch.empty_like(w), H,
                                    residual, act, stream)
 
 
+@_on_stream
 def lowrank_fwd_varlen(x, z, U, pos, W, H, residual=False, act=False, stream=None):
     return dsc_lowrank_fwd_varlen(x, z, U, pos, torch.empty_like(x), W, H, residual, act, stream)
 
 
+@_on_stream
 def lowrank_bwd_varlen(x, z, U, pos, dy, W, H, residual=False, act=False, workspace=None,
                        stream=None):
     if workspace is None:
@@ -608,6 +647,7 @@ def lowrank_bwd_varlen(x, z, U, pos, dy, W, H, residual=False, act=False, worksp
                                   torch.empty_like(U), workspace, W, H, residual, act, stream)
 
 
+@_on_stream
 def headwise_gen_fwd(x, xh, Mt, W, H, residual=False, act=False, stream=None):
     return dsc_headwise_gen_fwd(x, xh, Mt, torch.empty_like(x), W, H, residual, act, stream)
 
@@ -620,6 +660,7 @@ def scan_workspace(x, N, G):
     return x.new_empty(n, dtype=torch.uint8) if n else None
 
 
+@_on_stream
 def scan_fwd(x, delta, A, Bm, Cm, w=None, cb=None, Dk=None, z=None, dt_bias=None, h0=None,
              conv0=None, pos=None, residual=False, act=False, final_state=False, workspace=None,
              stream=None):
@@ -648,6 +689,7 @@ def scan_bwd_workspace(x, N, G):
     return x.new_empty(n, dtype=torch.uint8) if n else None
 
 
+@_on_stream
 def scan_bwd(x, delta, A, Bm, Cm, dy, w=None, cb=None, Dk=None, z=None, dt_bias=None, pos=None,
              residual=False, act=False, workspace=None, stream=None):
     """The gradients of scan_fwd by name: dx, ddelta, dA, dBm, dCm, and dw, dcb,
@@ -662,6 +704,7 @@ def scan_bwd(x, delta, A, Bm, Cm, dy, w=None, cb=None, Dk=None, z=None, dt_bias=
                         residual, act, stream)
 
 
+@_on_stream
 def scan_decode(x, delta, A, Bm, Cm, h, conv=None, w=None, cb=None, Dk=None, z=None,
                 dt_bias=None, residual=False, act=False, stream=None):
     y = x.new_empty(x.shape)
@@ -669,6 +712,7 @@ def scan_decode(x, delta, A, Bm, Cm, h, conv=None, w=None, cb=None, Dk=None, z=N
                            stream)
 
 
+@_on_stream
 def layernorm_fwd(x, w=None, b=None, eps=1e-5, stream=None):
     """y, mean, rstd of the rows of x (M, D)."""
     mean = x.new_empty(x.shape[0], dtype=torch.float32)
@@ -681,6 +725,7 @@ def layernorm_workspace(x):
     return x.new_empty(max(n, 1), dtype=torch.uint8)
 
 
+@_on_stream
 def layernorm_bwd(x, w, dy, mean, rstd, workspace=None, stream=None):
     """dx, dw, db (the latter two also where w is None: the gradients at w = 1, b = 0)."""
     if workspace is None:
