@@ -158,6 +158,8 @@ __global__ __launch_bounds__(kScanDecManyWaves * 64) void scan_decode_kernel(Sca
       for (int j = 0; j < NS; ++j) {
         h[i][j] = fmaf(__builtin_amdgcn_exp2f(dti * (A2[i][j] * kLog2e)), h[i][j],
                        dui * Bv[ONE ? 0 : i][j]);
+        // past N: zero times an infinite dt u would reach the sum
+        h[i][j] = j < have ? h[i][j] : 0.0f;
         p = fmaf(Cv[ONE ? 0 : i][j], h[i][j], p);
       }
       p = join<L>(p);

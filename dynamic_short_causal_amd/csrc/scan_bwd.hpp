@@ -330,7 +330,10 @@ template <bool TIGHT> __device__ __forceinline__ int in_loop(int v) {
   return v;
 }
 
-template <typename E, int NS, int NW, int WM, bool PACKED>
+// RAGGED: N is not a multiple of NS.  The states past N then stay zero, which dt u
+// or dp times their zero B or C do not where they are infinite.  In the same kernel
+// the selects for that would cost a whole N 1 %: 8 x 4096 x 1536, N = 16, bf16.
+template <typename E, int NS, int NW, int WM, bool PACKED, bool RAGGED>
 __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(scan_bwd_occupancy(sizeof(E), NW, WM))))
     void scan_bwd_kernel(ScanBwdP p) {
@@ -456,6 +459,10 @@ __global__ __launch_bounds__(64 * NW)
     if constexpr (PACKED) starts = tile_starts(a, at.b, t, t1, TT, lane);
     __syncthreads();
     if (have > 0) {
+      if constexpr (RAGGED) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) hs[j] = j < have ? hs[j] : 0.0f;
+      }
       // the tile's states, then q through them backwards
       float hist[TT][NS];
 #pragma unroll
@@ -469,6 +476,7 @@ __global__ __launch_bounds__(64 * NW)
         for (int j = 0; j < NS; ++j) {
           const float hp = i ? hist[i > 0 ? i - 1 : 0][j] : hs[j];
           hist[i][j] = fmaf(__builtin_amdgcn_exp2f(dtv * A2[j]), start ? 0.0f : hp, duv * bc[j]);
+          if constexpr (RAGGED) hist[i][j] = j < have ? hist[i][j] : 0.0f;
           o = fmaf(bc[NS + j], hist[i][j], o);
         }
         s_part[0][wave][i][lane] = o;
@@ -485,11 +493,12 @@ __global__ __launch_bounds__(64 * NW)
         for (int j = 0; j < NS; ++j) {
           const float hp = i ? hist[i > 0 ? i - 1 : 0][j] : hs[j];
           q[j] = fmaf(bc[NS + j], dpv, q[j]);
+          if constexpr (RAGGED) q[j] = j < have ? q[j] : 0.0f;
           sums[j] = dpv * hist[i][j];
           sums[NS + j] = q[j] * duv;
           e = fmaf(q[j], bc[j], e);
           const float qa = q[j] * __builtin_amdgcn_exp2f(dtv * A2[j]);
-          q[j] = start ? 0.0f : qa;
+          q[j] = start || (RAGGED && j >= have) ? 0.0f : qa;
           const float r = start ? 0.0f : q[j] * hp;
           dA[j] = fmaf(r, dtv, dA[j]);
           ss = fmaf(r, A2[j], ss);
@@ -653,7 +662,10 @@ static hipError_t scan_bwd_run(const ScanBwdP &p, int64_t groups) {
     hipLaunchKernelGGL((scan_bwd_sums_kernel<E, NS, NW, WM, PACKED, false>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED>), grid, block, 0, s, p);
+  if (p.a.N % NS)
+    hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, false>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

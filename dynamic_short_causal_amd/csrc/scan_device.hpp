@@ -148,7 +148,9 @@ __device__ __forceinline__ void st_at(E *base, uint32_t off, const float (&o)[N]
 
 // ---- B and C of a tile ------------------------------------------------------
 // In LDS as fp32: [token][group] runs of 2 NS, the B of a group's NS states, then
-// their C; states past N and tokens past the end are zero.  The lanes of a group
+// their C; tokens past the end are zero.  States past N are zero, too, or with
+// COPY further copies of the first ones, among which a state's C is shared out.
+// The lanes of a group
 // (in the backward a whole wave) read the same run, a broadcast, in order with
 // their other LDS reads.  Scalar loads
 // from memory were measured instead: unpacking and addressing took as many
@@ -178,7 +180,11 @@ __device__ __forceinline__ void bc_at(int tid, int k, int &row, int &which, int 
   n0 = group * NS + i % NS;
 }
 
-template <typename E, int NS, int NW, int TT, int TH = 64 * NW>
+// The state that place n < Np stands for, where places past N hold copies: Np is
+// below 2 N, or four (N = 1), so a state has one, two or four places.
+__device__ __forceinline__ int copy_of(int n, int N) { return n < N ? n : n % N; }
+
+template <typename E, int NS, int NW, int TT, int TH = 64 * NW, bool COPY = false>
 __device__ __forceinline__ void ld_bc(const ScanArgs &a, int b, int g, int t, int t1,
                                       BcRaw<E, NS, NW, TT, TH> &o, int tid = (int)threadIdx.x) {
   typedef BcGeo<NS, NW, TT, TH> G;
@@ -189,25 +195,32 @@ __device__ __forceinline__ void ld_bc(const ScanArgs &a, int b, int g, int t, in
     for (int i = 0; i < RowBits<E, G::QN>::dwords; ++i) r.d[i] = 0u;
     int row, which, n0, at;
     bc_at<NS, NW, TT, TH>(tid, k, row, which, n0, at);
-    if (t + row >= t1 || n0 >= a.N) continue;
+    if (t + row >= t1) continue;
+    if constexpr (COPY) {
+      // a run of four states with N a multiple of four: all its own, or all copies
+      if (a.bc_vec && n0 >= a.N) n0 -= a.N;
+    } else if (n0 >= a.N) {
+      continue;
+    }
     const int64_t tok = (int64_t)b * a.T + t + row;
     const E *p = (which ? (const E *)a.Cm + tok * a.c_row : (const E *)a.Bm + tok * a.b_row) +
-                 g * a.N + n0;
+                 g * a.N;
     if (a.bc_vec) {
-      r = ld_row<E, G::QN>(p);
+      r = ld_row<E, G::QN>(p + n0);
     } else {
 #pragma unroll
       for (int j = 0; j < G::QN; ++j)
-        if (n0 + j < a.N) {
-          if constexpr (sizeof(E) == 2) r.d[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
-          else r.d[j] = __float_as_uint(p[j]);
+        if (COPY || n0 + j < a.N) {
+          const E v = p[COPY ? copy_of(n0 + j, a.N) : n0 + j];
+          if constexpr (sizeof(E) == 2) r.d[j >> 1] |= (uint32_t)v << (16 * (j & 1));
+          else r.d[j] = __float_as_uint(v);
         }
     }
   }
 }
 
-template <typename E, int NS, int NW, int TT, int TH = 64 * NW>
-__device__ __forceinline__ void st_bc(const BcRaw<E, NS, NW, TT, TH> &o, float *s_bc) {
+template <typename E, int NS, int NW, int TT, int TH = 64 * NW, bool COPY = false>
+__device__ __forceinline__ void st_bc(const BcRaw<E, NS, NW, TT, TH> &o, float *s_bc, int N = 0) {
   typedef BcGeo<NS, NW, TT, TH> G;
 #pragma unroll
   for (int k = 0; k < G::NQ; ++k) {
@@ -215,6 +228,14 @@ __device__ __forceinline__ void st_bc(const BcRaw<E, NS, NW, TT, TH> &o, float *
     bc_at<NS, NW, TT, TH>((int)threadIdx.x, k, row, which, n0, at);
     float v[G::QN];
     unpack_row<E, G::QN>(o.q[k], v);
+    if constexpr (COPY) {
+      if (N < NS * NW && which) {
+        const float part = N == 1 ? 0.25f : 0.5f;  // exact
+#pragma unroll
+        for (int j = 0; j < G::QN; ++j)
+          if (n0 + j >= N || n0 + j + N < NS * NW) v[j] *= part;
+      }
+    }
     st_row<float, G::QN>(s_bc + at, v);
   }
 }

@@ -24,7 +24,7 @@ def test_the_scan_backward_does_not_spill(builder, source):
     _, _, remarks = builder._compile(unit)
     rows = builder._resources(remarks)
     main = [r for r in rows if "scan_bwd_kernel" in r["name"]]
-    assert len(main) == 4
+    assert len(main) == 8
     assert {r["name"]: r["ScratchSize [bytes/lane]"] for r in rows} == \
         {r["name"]: "0" for r in rows}
 
