@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kScanDecManyWaves * 64) void scan_decode_kernel(Sca
     }
   }
   if (mine) {
-    ((E *)a.y)[b * a.D + c] = to_elem<E>(fmaf(dk, u, o) * z);
+    ((E *)a.y)[b * a.D + c] = to_elem<E>((a.Dk ? fmaf(dk, u, o) : o) * z);
 #pragma unroll
     for (int k = 2; k < WT; ++k)  // the inputs slide by one token
       if (k < a.W) cp[(int64_t)(S - k) * a.D] = cv[k - 2];

@@ -560,7 +560,7 @@ __global__ __launch_bounds__(64 * NW)
           // sum[2] holds A log2(e) r
           const float ddt = fmaf(k.u[i][j], sum[1][j], sum[2][j] * 0.6931471805599453f);
           ddelta[j] = on ? ddt * sigmoid_f(k.v[i][j]) : 0.0f;
-          du[i][j] = on ? fmaf(k.dt[i][j], sum[1][j], dk[j] * k.dp[i][j]) : 0.0f;
+          du[i][j] = on ? fmaf(k.dt[i][j], sum[1][j], a.Dk ? dk[j] * k.dp[i][j] : 0.0f) : 0.0f;
           ds[i][j] = du[i][j];
         }
         if (a.act && on) {
@@ -576,7 +576,7 @@ __global__ __launch_bounds__(64 * NW)
             unpack_row<E, PV>(dyr[i], dz);
 #pragma unroll
             for (int j = 0; j < PV; ++j)
-              dz[j] *= fmaf(dk[j], k.u[i][j], sum[0][j]) * silu_grad_f(z[j]);
+              dz[j] *= (a.Dk ? fmaf(dk[j], k.u[i][j], sum[0][j]) : sum[0][j]) * silu_grad_f(z[j]);
             st_at<E, PV>((E *)a.dz + n, off.d, dz);
           }
 #pragma unroll

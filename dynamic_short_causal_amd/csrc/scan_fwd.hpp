@@ -162,6 +162,11 @@ __global__ __launch_bounds__(64 * scan_fwd_waves(GR))
     s_par[1][i] = on && a.dtb ? a.dtb[at.c0 + i] : 0.0f;
     s_par[2][i] = on && a.Dk ? a.Dk[at.c0 + i] : 0.0f;
   }
+  // what u is held to where Dk multiplies it: without Dk an infinite u adds nothing.
+  // (An undefined u has made the sum undefined.)  A select on the pointer would
+  // take the one register more that the kernel for N = 16 does not have.
+  __shared__ float s_most;
+  if (threadIdx.x == 0) s_most = a.Dk ? __builtin_inff() : 0.0f;
   ScanRaw<E, PV, NI, WM> raw;
   BcRaw<E, NS, GR, TT, TH> bcr;
   const ScanOff off = scan_off(a, r0, w0);
@@ -304,8 +309,10 @@ __global__ __launch_bounds__(64 * scan_fwd_waves(GR))
           if (t + r0 + i < t1) {
             float o[PV];
             ld_lds<PV>(&s_du[wave][r0 + i][v0], o);
+            const float most = s_most;
 #pragma unroll
-            for (int j = 0; j < PV; ++j) o[j] = fmaf(dk[j], u[i][j], o[j]);
+            for (int j = 0; j < PV; ++j)
+              o[j] = fmaf(dk[j], __builtin_amdgcn_fmed3f(u[i][j], -most, most), o[j]);
             if (gate) {
               float zv[PV];
               unpack_row<E, PV>(zr[i], zv);

@@ -75,11 +75,12 @@ def kinds(a):
     return np.where(np.isnan(a), 2, np.where(np.isinf(a), np.sign(a), 0)).astype(int)
 
 
-def positive(B, T, D, N, dtype, seed):
+def positive(B, T, D, N, dtype, seed, Dk=True, z=False):
     """Inputs whose products keep their sign, rates that decay slowly."""
-    p = make(B, T, D, N, 0, 1, dtype, seed, z=False)
-    for k in ("x", "Bm", "Cm", "Dk"):
-        p[k] = p[k].abs() + 0.5
+    p = make(B, T, D, N, 0, 1, dtype, seed, z=z, Dk=Dk)
+    for k in ("x", "Bm", "Cm", "Dk", "z"):
+        if k in p:
+            p[k] = p[k].abs() + 0.5
     p["A"] = -0.01 * (1.0 + torch.arange(N).float()).repeat(D, 1)
     return p
 
@@ -136,3 +137,40 @@ def test_an_infinite_gradient(dsc, B, T, N, dtype):
     assert (kinds(want["dx"])[0, :22, 3] == 1).all() and np.abs(kinds(want["dx"])).sum() == 22
     for k in ("dx", "ddelta", "dBm", "dCm"):
         assert np.array_equal(kinds(g[k]), kinds(want[k])), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("N", [5, 16])
+def test_an_absent_Dk_adds_nothing(dsc, N, z, dtype):
+    """Without Dk, an infinite u or dp meets no zero in its place."""
+    B, T, D = 1, 40, 16
+    p = positive(B, T, D, N, dtype, 2800 + N, Dk=False, z=z)
+    p["x"][0, 21, 3] = float("inf")
+    q = f64(p)
+    with np.errstate(all="ignore"):
+        want, hw, _ = ref.scan_fwd(**q)
+    assert (kinds(want)[0, 21:, 3] == 1).all()
+    y, h, _ = dsc.scan_fwd(**dev(p), final_state=True)
+    assert np.array_equal(kinds(y), kinds(want)) and np.array_equal(kinds(h), kinds(hw))
+    seq = {k: v for k, v in dev(p).items() if v.dim() >= 3}
+    tok = {k: v[:, 21] for k, v in seq.items()}
+    hd = torch.zeros(B, D, N, device=gu.dev())
+    y = dsc.scan_decode(**dict(dev(p), **tok), h=hd)
+    assert kinds(y)[0, 3] == 1 and np.abs(kinds(y)).sum() == 1
+    dy = di.randn((B, T, D), 1.0, 2900, "bf16" if dtype == BF16 else "f32")
+    g = dsc.scan_bwd(**dev(p), dy=dy.to(gu.dev()))
+    with np.errstate(all="ignore"):
+        want = ref.scan_bwd(**q, dy=gu.f64(dy))
+    if z:
+        assert np.array_equal(kinds(g["dz"]), kinds(want["dz"]))
+        assert (np.abs(kinds(want["dz"])[0, 21:, 3]) == 1).all()
+    # an infinite gradient
+    p = positive(B, T, D, N, dtype, 2850 + N, Dk=False, z=z)
+    dy[0, 21, 3] = float("inf")
+    g = dsc.scan_bwd(**dev(p), dy=dy.to(gu.dev()))
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        want = ref.scan_bwd(**f64(p), dy=gu.f64(dy))
+    assert np.array_equal(kinds(g["dx"]), kinds(want["dx"]))
+    assert (kinds(want["dx"])[0, :22, 3] == 1).all()
