@@ -682,10 +682,13 @@ def scan_fwd(x, delta, A, Bm, Cm, w=None, cb=None, Dk=None, z=None, dt_bias=None
     return (y, hT, convT) if final_state else y
 
 
-def scan_bwd_workspace(x, N, G):
+def scan_bwd_workspace(x, N, G, W=None):
+    """Workspace of scan_bwd with W taps, or (None) with any number of them."""
     B, T, D = x.shape
-    s = ScanShape(B=B, T=T, D=D, N=N, G=G, dtype=_dtype(x))
-    n = int(LIB.dsc_scan_bwd_workspace_bytes(_shape_ptr(s)))
+    n = 0
+    for taps in (0, 8) if W is None else (W,):
+        s = ScanShape(B=B, T=T, D=D, N=N, G=G, W=taps, dtype=_dtype(x))
+        n = max(n, int(LIB.dsc_scan_bwd_workspace_bytes(_shape_ptr(s))))
     return x.new_empty(n, dtype=torch.uint8) if n else None
 
 
@@ -695,7 +698,8 @@ def scan_bwd(x, delta, A, Bm, Cm, dy, w=None, cb=None, Dk=None, z=None, dt_bias=
     """The gradients of scan_fwd by name: dx, ddelta, dA, dBm, dCm, and dw, dcb,
     dDk, dz, ddt_bias of the inputs given."""
     if workspace is None:
-        workspace = scan_bwd_workspace(x, A.shape[-1], Bm.shape[-2])
+        workspace = scan_bwd_workspace(x, A.shape[-1], Bm.shape[-2],
+                                       0 if w is None else w.shape[-1])
     inputs = dict(dx=x, ddelta=delta, dA=A, dBm=Bm, dCm=Cm, dw=w, dcb=cb, dDk=Dk, dz=z,
                   ddt_bias=dt_bias)
     grads = {n: t.new_empty(t.shape)

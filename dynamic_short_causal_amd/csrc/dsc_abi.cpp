@@ -539,8 +539,9 @@ static Span param_span(const char *name, const void *p, int64_t elems, int esize
 }
 
 // Sizes, dtype, flags and strides of a scan call; fills in *a (the strides of
-// dense rows among it).
-static dsc_status scan_check(const dsc_scan_shape *s, dsc::ScanArgs *a) {
+// dense rows among it) and the tiling of a forward or a backward call.
+static dsc_status scan_check(const dsc_scan_shape *s, dsc::ScanArgs *a, dsc::ScanPlan *fwd,
+                             dsc::ScanBwdPlan *bwd) {
   if (s == nullptr) return fail(DSC_ERR_INVALID_ARG, "shape is NULL");
   int V = 0;
   dsc_status st = check_common(s->B, s->T, s->D, s->W == 0 ? 1 : s->W, 1, (dsc_dtype)s->dtype,
@@ -580,13 +581,20 @@ static dsc_status scan_check(const dsc_scan_shape *s, dsc::ScanArgs *a) {
   a->bf16 = s->dtype == DSC_BF16;
   a->residual = (s->flags & DSC_RESIDUAL) != 0;
   a->act = (s->flags & DSC_ACT_SILU) != 0;
-  // workgroups of the forward, of the backward, its last launch and a decode step
-  const dsc::ScanPlan p = dsc::scan_plan(s->B, s->T, s->D, s->G, s->N);
-  const dsc::ScanBwdPlan q = dsc::scan_bwd_plan(s->B, s->T, s->D, s->G, s->N);
-  const int64_t fin = s->B * s->T * GN / 128 + s->D * (s->N + 12) / 256 + 8 +
-                      s->B * q.nc * 7 * s->D / 256;
-  if (p.cols * p.nc > INT32_MAX || q.cols * q.nc > INT32_MAX || fin > INT32_MAX ||
-      s->B * s->D / 16 > INT32_MAX)
+  // workgroups of a decode step, of the forward, of the backward and its last launch
+  int64_t groups = s->B * s->D / 16;
+  if (fwd) {
+    *fwd = dsc::scan_plan(s->B, s->T, s->D, s->G, s->N);
+    groups = fwd->cols * fwd->nc;
+  }
+  if (bwd) {
+    *bwd = dsc::scan_bwd_plan(s->B, s->T, s->D, s->G, s->N, s->W, a->bf16);
+    const int64_t fin = s->B * s->T * GN / 128 + s->D * (s->N + 12) / 256 + 8 +
+                        s->B * bwd->nc * 7 * s->D / 256;
+    groups = bwd->cols * bwd->nc;
+    if (groups < fin) groups = fin;
+  }
+  if (groups > INT32_MAX)
     return fail(DSC_ERR_INVALID_ARG, "the call needs more than 2^31 - 1 workgroups");
   return DSC_OK;
 }
@@ -610,8 +618,8 @@ static dsc_status need_workspace(const void *workspace, size_t bytes, size_t nee
 
 size_t dsc_scan_fwd_workspace_bytes(const dsc_scan_shape *shape) {
   dsc::ScanArgs a{};
-  if (scan_check(shape, &a) != DSC_OK || a.B == 0 || a.T == 0) return 0;
-  return dsc::scan_plan(a.B, a.T, a.D, a.G, a.N).total * sizeof(float);
+  dsc::ScanPlan p{};
+  return scan_check(shape, &a, &p, nullptr) == DSC_OK ? p.total * sizeof(float) : 0;
 }
 
 dsc_status dsc_scan_fwd(const dsc_scan_shape *shape, const void *x, const void *delta,
@@ -621,13 +629,14 @@ dsc_status dsc_scan_fwd(const dsc_scan_shape *shape, const void *x, const void *
                         float *hT, void *convT, void *workspace, size_t workspace_bytes,
                         void *stream) {
   dsc::ScanArgs a{};
-  dsc_status st = scan_check(shape, &a);
+  dsc::ScanPlan p{};
+  dsc_status st = scan_check(shape, &a, &p, nullptr);
   if (st != DSC_OK) return st;
   const int es = a.bf16 ? 2 : 4;
   const int64_t n = a.B * a.T, GN = (int64_t)a.G * a.N, nh = a.B * a.D * a.N;
   const int64_t nconv = a.W > 1 ? a.B * (a.W - 1) * a.D : 0;
   const bool empty = n == 0;
-  const size_t need = dsc::scan_plan(a.B, a.T, a.D, a.G, a.N).total * sizeof(float);
+  const size_t need = p.total * sizeof(float);
   if ((st = need_workspace(workspace, workspace_bytes, need)) != DSC_OK) return st;
   const Span s[] = {
       rows_span("x", x, n, a.x_row, a.D, es, 16),
@@ -657,7 +666,7 @@ dsc_status dsc_scan_decode(const dsc_scan_shape *shape, const void *x, const voi
                            const void *cb, const float *Dk, const void *z,
                            const float *dt_bias, float *h, void *conv, void *y, void *stream) {
   dsc::ScanArgs a{};
-  dsc_status st = scan_check(shape, &a);
+  dsc_status st = scan_check(shape, &a, nullptr, nullptr);
   if (st != DSC_OK) return st;
   if (a.T != 1) return fail(DSC_ERR_INVALID_ARG, "T=%lld: a decode step takes one token",
                             (long long)a.T);
@@ -686,8 +695,8 @@ dsc_status dsc_scan_decode(const dsc_scan_shape *shape, const void *x, const voi
 
 size_t dsc_scan_bwd_workspace_bytes(const dsc_scan_shape *shape) {
   dsc::ScanArgs a{};
-  if (scan_check(shape, &a) != DSC_OK) return 0;
-  return dsc::scan_bwd_plan(a.B, a.T, a.D, a.G, a.N).total * sizeof(float);
+  dsc::ScanBwdPlan p{};
+  return scan_check(shape, &a, nullptr, &p) == DSC_OK ? p.total * sizeof(float) : 0;
 }
 
 dsc_status dsc_scan_bwd(const dsc_scan_shape *shape, const void *x, const void *delta,
@@ -698,11 +707,12 @@ dsc_status dsc_scan_bwd(const dsc_scan_shape *shape, const void *x, const void *
                         float *ddt_bias, void *workspace, size_t workspace_bytes,
                         void *stream) {
   dsc::ScanArgs a{};
-  dsc_status st = scan_check(shape, &a);
+  dsc::ScanBwdPlan p{};
+  dsc_status st = scan_check(shape, &a, nullptr, &p);
   if (st != DSC_OK) return st;
   const int es = a.bf16 ? 2 : 4;
   const int64_t n = a.B * a.T, GN = (int64_t)a.G * a.N, act = n * a.D;
-  const size_t need = dsc::scan_bwd_plan(a.B, a.T, a.D, a.G, a.N).total * sizeof(float);
+  const size_t need = p.total * sizeof(float);
   if ((st = need_workspace(workspace, workspace_bytes, need)) != DSC_OK) return st;
   const Span s[] = {
       rows_span("x", x, n, a.x_row, a.D, es, 16),

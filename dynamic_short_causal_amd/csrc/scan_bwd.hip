@@ -100,7 +100,7 @@ __global__ __launch_bounds__(kScanFinThreads) void scan_bwd_finish_kernel(ScanBw
 template <typename E, int NS, int NW> hipError_t scan_bwd_nw(const ScanBwdP &, int64_t);
 
 template <typename E> static hipError_t bwd(const ScanArgs &a) {
-  const ScanBwdPlan pl = scan_bwd_plan(a.B, a.T, a.D, a.G, a.N);
+  const ScanBwdPlan pl = scan_bwd_plan(a.B, a.T, a.D, a.G, a.N, a.W, a.bf16);
   ScanBwdP p{};
   p.a = a;
   p.dg = (int)(a.D / a.G);

@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_sums_kernel(ScanBwdP p) {
 // eight taps 733 and 1031 us.  fp32 with eight taps does not fit: 1110 us with
 // the rest in memory, 1052 us with one workgroup.
 constexpr int scan_bwd_occupancy(int esize, int nw, int wm) {
-  return nw == 4 && (esize == 2 || wm <= 4) ? 2 : 1;
+  return nw == 4 ? scan_bwd_resident(esize == 2, nw, wm) : 1;
 }
 // Those that fit only without the addresses and values that can be had again
 // where they are used.  The compiler would put 60 to 100 bytes a lane into memory

@@ -120,6 +120,40 @@ constexpr int kScanParV = 3 + kScanMaxW;
 // of 8 tokens, 748 and 1202 us with 16.
 constexpr int scan_bwd_tile(int ns, int nw) { return ns == 8 || nw <= 2 ? 8 : 16; }
 
+// Workgroups of the backward's main launch that a CU holds at once, by its
+// registers and LDS.
+constexpr int scan_bwd_resident(bool bf16, int nw, int W) {
+  const bool full = !bf16 && W > 4;  // fp32 with more than four taps: above 256 registers
+  return nw >= 8 ? 1 : nw == 4 ? (full ? 1 : 2) : nw == 2 ? (full ? 2 : 4) : 4;
+}
+
+// Chunks of the backward's time axis for `cols` columns of workgroups.  k chunks
+// of n tiles each take cols k / slots rounds of resident workgroups, rounded up,
+// and a round takes the time of n tiles; in a cut call of one tile more, for
+// starting and for what the chunks hand on, and of a twentieth of a tile for every
+// chunk, whose states each workgroup folds.  The least of that product, among the
+// k that rounding leaves as they are.  Measured at 40 sizes with 1 to 64 chunks:
+// 1.1 % above the best of them in the mean, 14 % at most (74 us against 65).
+// N = 16, bf16: 8 x 4096 x 1536 (0.38 rounds whole) 1292 us in eight, 1409 in five,
+// 2436 whole; 8 x 2048 x 1088 (0.27) 523 in eleven, 542 in seven, 573 in eight;
+// 24 x 2048 x 1536 (1.13) 1902 in eight, 1998 in five, 2517 whole; 32 x 2048 x 1536
+// (1.5) 2529 in two, 2549 whole, 2522 in eight; 1 x 4096 x 512 114 in 64, 123 in 32.
+inline int64_t scan_bwd_chunks(int64_t cols, int64_t slots, int64_t tiles) {
+  int64_t best = 1;
+  double least = 0.0;
+  for (int64_t k = 1; k <= 64 && k <= tiles; ++k) {
+    const int64_t n = (tiles + k - 1) / k;
+    if ((tiles + n - 1) / n != k) continue;
+    const int64_t rounds = (cols * k + slots - 1) / slots;
+    const double t = (double)rounds * ((double)n + (k > 1 ? 1.0 + 0.05 * (double)k : 0.0));
+    if (k == 1 || t < least) {
+      least = t;
+      best = k;
+    }
+  }
+  return best;
+}
+
 // Tiling of the backward and its workspace, in floats from the start.
 struct ScanBwdPlan {
   int ns, nw, nblk, tc, nc, tiles;
@@ -127,7 +161,8 @@ struct ScanBwdPlan {
   size_t ck, cum, hend, qend, sdt, dbc, pA, pV, tail, head, total;
 };
 
-inline ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D, int G, int N) {
+inline ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D, int G, int N, int W,
+                                 bool bf16) {
   ScanBwdPlan p{};
   // 16 waves of four states would have 128 registers each, too few
   p.ns = N > 32 ? 8 : 4;
@@ -137,34 +172,8 @@ inline ScanBwdPlan scan_bwd_plan(int64_t B, int64_t T, int64_t D, int G, int N) 
   p.cols = B * G * p.nblk;
   const int tile = scan_bwd_tile(p.ns, p.nw);
   const int64_t tiles = (T + tile - 1) / tile;
-  // Resident workgroups a CU, by the registers and LDS of the main launch; rounds
-  // of workgroups are those of a grid over these slots.  The axis stays whole
-  // where its last round is 91 % full: a cut call's first launch also needs what
-  // the chunks hand back.  Else eight chunks, where they make 1.8 rounds, or the
-  // fewest, of a tile at least, whose last round is 90 % full.  Measured in bf16,
-  // T = 2048, D = 1536, N = 16: B = 64 (3 rounds) 4546 us whole, 4984 us in
-  // eight; B = 43 (2.02) 3852 and 3387; B = 24 (1.13) 1871 in eight, 1867 to
-  // 1990 in four to sixteen; B = 8 (0.38) 657 in eight, 707 in five (1.88
-  // rounds); B = 3 (0.14) 278 in seven (0.98 rounds), 357 in eight.  N = 8, B = 8
-  // (0.19): 492 in five (0.94 rounds), 542 in eight (1.5).  2 x 333 x 520 fp32,
-  // 21 tiles: 54 us with chunks of one tile, 64 of two, 85 of four.
-  const int64_t slots = kCUs * (p.nw >= 8 ? 1 : p.nw == 4 ? 2 : 4);
-  auto full = [&p, slots](int64_t k) {
-    const int64_t wg = p.cols * k, rounds = (wg + slots - 1) / slots;
-    return (double)wg / (double)(rounds * slots);
-  };
-  int64_t nc = 1;
-  if (p.cols > 0 && full(1) < 0.91) {
-    if (p.cols * 40 >= slots * 9) {
-      nc = tiles < 8 ? tiles : 8;
-    } else {
-      for (int64_t k = 2; k <= 64 && k <= tiles; ++k) {
-        if (full(k) > full(nc) + 1e-9) nc = k;
-        if (full(k) >= 0.9) break;
-      }
-    }
-  }
-  if (nc < 1) nc = 1;
+  const int64_t nc = scan_bwd_chunks(p.cols, (int64_t)kCUs * scan_bwd_resident(bf16, p.nw, W),
+                                     tiles);
   const int64_t per = tiles > 0 ? (tiles + nc - 1) / nc : 1;
   p.tc = (int)(per * tile);
   p.nc = (int)(tiles > 0 ? (tiles + per - 1) / per : 1);
