@@ -11,6 +11,7 @@
 // forward 16384 x 6144 bf16 69 us, 5.8 TB/s; backward 16384 x 2048 bf16 41 us,
 // 4.9 TB/s (37 us and 4 us for the sums of the partials), 999 x 8192 fp32 27 us.
 #include "dsc_device.hpp"
+#include "grid_slices.hpp"
 #include "norm_launch.hpp"
 
 namespace dsc {
@@ -46,11 +47,11 @@ template <typename E> __device__ __forceinline__ void ld_vec(const void *p, int6
 // Forward, VPT vectors of a row a thread, TPR threads a row
 // ---------------------------------------------------------------------------
 template <typename E, int TPR, int VPT>
-__global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a) {
+__global__ __launch_bounds__(kLnThreads) void ln_fwd_kernel(LnArgs a, uint32_t first) {
   constexpr int V = Vw<E>::n;
   __shared__ float red[2][kLnThreads / 64];
   const int tid = (int)threadIdx.x % TPR;
-  const int64_t m = (int64_t)blockIdx.x * (kLnThreads / TPR) + threadIdx.x / TPR;
+  const int64_t m = ((int64_t)blockIdx.x + first) * (kLnThreads / TPR) + threadIdx.x / TPR;
   if (TPR == 64 && m >= a.M) return;  // whole waves; a workgroup's single row always exists
   const int nvec = (int)(a.D / V);
   const E *x = (const E *)a.x + m * a.D;
@@ -462,10 +463,10 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_long_cols_kernel(LnArgs a) 
 // workgroup takes 32 columns; 8 threads of four columns each make a row of it,
 // 32 rows at a time, whose sums are added in order at the end.
 template <typename E>
-__global__ __launch_bounds__(256) void ln_reduce_kernel(LnArgs a, int64_t parts) {
+__global__ __launch_bounds__(256) void ln_reduce_kernel(LnArgs a, int64_t parts, uint32_t first) {
   __shared__ __align__(16) float red[32][32];
   const int q = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const int64_t col = (int64_t)blockIdx.x * 32 + q * 4, cols = 2 * a.D;
+  const int64_t col = ((int64_t)blockIdx.x + first) * 32 + q * 4, cols = 2 * a.D;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < cols) {
 #pragma unroll 8
@@ -476,7 +477,7 @@ __global__ __launch_bounds__(256) void ln_reduce_kernel(LnArgs a, int64_t parts)
   }
   *reinterpret_cast<float4 *>(&red[g][q * 4]) = s;
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  const int64_t c = ((int64_t)blockIdx.x + first) * 32 + threadIdx.x;
   if (threadIdx.x < 32 && c < cols) {
     float t = 0.0f;
 #pragma unroll
@@ -500,9 +501,10 @@ constexpr int64_t kLnWaveVecs = 4 * 64;
 
 template <typename E, int TPR, int VPT> static hipError_t ln_fwd_go(const LnArgs &a) {
   constexpr int rows = kLnThreads / TPR;
-  hipLaunchKernelGGL((ln_fwd_kernel<E, TPR, VPT>), dim3((unsigned)((a.M + rows - 1) / rows)),
-                     dim3(kLnThreads), 0, (hipStream_t)a.stream, a);
-  return hipGetLastError();
+  return launch_slices((a.M + rows - 1) / rows, kLnThreads, [&](uint32_t first, dim3 grid) {
+    hipLaunchKernelGGL((ln_fwd_kernel<E, TPR, VPT>), grid, dim3(kLnThreads), 0,
+                       (hipStream_t)a.stream, a, first);
+  });
 }
 
 template <typename E, int TPR> static hipError_t ln_fwd_vpt(const LnArgs &a, int64_t vpt) {
@@ -572,9 +574,10 @@ template <typename E> static hipError_t ln_bwd(const LnArgs &a) {
     if (e != hipSuccess) return e;
   }
   if (!a.dw) return hipSuccess;
-  hipLaunchKernelGGL((ln_reduce_kernel<E>), dim3((unsigned)((2 * a.D + 31) / 32)), dim3(256), 0,
-                     (hipStream_t)a.stream, a, ln_bwd_groups(a.M, a.D, a.bf16));
-  return hipGetLastError();
+  return launch_slices((2 * a.D + 31) / 32, 256, [&](uint32_t first, dim3 grid) {
+    hipLaunchKernelGGL((ln_reduce_kernel<E>), grid, dim3(256), 0, (hipStream_t)a.stream, a,
+                       ln_bwd_groups(a.M, a.D, a.bf16), first);
+  });
 }
 
 hipError_t ln_fwd_launch(const LnArgs &a) { return a.bf16 ? ln_fwd<bf16>(a) : ln_fwd<float>(a); }

@@ -8,7 +8,7 @@ template <typename E, int NS, int NW> hipError_t scan_fwd_nw(const ScanP &, int6
 template <typename E> static hipError_t fwd(const ScanArgs &a) {
   if (a.B == 0 || a.T == 0) return hipSuccess;
   const ScanPlan pl = scan_plan(a.B, a.T, a.D, a.G, a.N);
-  const ScanP p{a, a.ws + pl.hend, a.ws + pl.sdt, (int)(a.D / a.G), pl.nblk, pl.nc, pl.tc};
+  const ScanP p{a, a.ws + pl.hend, a.ws + pl.sdt, (int)(a.D / a.G), pl.nblk, pl.nc, pl.tc, 0};
   const int64_t groups = pl.cols * pl.nc;
   if (pl.ns == 2) {
     switch (pl.nw) {
@@ -69,10 +69,11 @@ template <int L> __device__ __forceinline__ float join(float v) {
 }
 
 template <typename E, int L, bool ONE>
-__global__ __launch_bounds__(kScanDecManyWaves * 64) void scan_decode_kernel(ScanArgs a) {
+__global__ __launch_bounds__(kScanDecManyWaves * 64) void scan_decode_kernel(ScanArgs a,
+                                                                            uint32_t first) {
   constexpr int NS = 4, WT = kScanMaxW, CP = 64 / L, LB = L < 4 ? L : 4;
   const int lane = (int)threadIdx.x & 63, q = lane % L, n0 = q * NS;
-  const int64_t wid = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+  const int64_t wid = ((int64_t)blockIdx.x + first) * (blockDim.x >> 6) + (threadIdx.x >> 6);
   const int64_t cols = (a.D + 63) / 64, b = wid / cols, c0 = (wid - b * cols) * 64;
   if (b >= a.B) return;  // whole waves; nothing is shared between them
   const int have = a.N - n0, S = a.W - 1;
@@ -188,9 +189,10 @@ __global__ __launch_bounds__(kScanDecManyWaves * 64) void scan_decode_kernel(Sca
 template <typename E, int L, bool ONE> static hipError_t dec(const ScanArgs &a) {
   const int64_t n = a.B * ((a.D + 63) / 64);
   const int wv = n >= (int64_t)kScanDecManyWaves * kCUs ? kScanDecManyWaves : kScanDecWaves;
-  hipLaunchKernelGGL((scan_decode_kernel<E, L, ONE>), dim3((unsigned)((n + wv - 1) / wv)),
-                     dim3(wv * 64), 0, (hipStream_t)a.stream, a);
-  return hipGetLastError();
+  return launch_slices((n + wv - 1) / wv, wv * 64, [&](uint32_t first, dim3 grid) {
+    hipLaunchKernelGGL((scan_decode_kernel<E, L, ONE>), grid, dim3(wv * 64), 0,
+                       (hipStream_t)a.stream, a, first);
+  });
 }
 
 template <typename E, bool ONE> static hipError_t dec_l(const ScanArgs &a) {

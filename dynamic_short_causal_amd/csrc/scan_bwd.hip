@@ -20,7 +20,7 @@ struct ScanFin {
 template <typename E>
 __global__ __launch_bounds__(kScanFinThreads) void scan_bwd_finish_kernel(ScanBwdP p, ScanFin f) {
   const ScanArgs &a = p.a;
-  int64_t blk = blockIdx.x;
+  int64_t blk = (int64_t)blockIdx.x + p.first;
   const int64_t BT = a.B * a.T;
   if (blk < f.bc) {
     int64_t i = blk * kScanFinThreads + threadIdx.x;
@@ -135,9 +135,12 @@ template <typename E> static hipError_t bwd(const ScanArgs &a) {
   f.seam = any && a.W > 1 ? blocks(a.B * (pl.nc - 1) * (a.W - 1) * a.D) : 0;
   f.np = pl.ns * pl.nw;
   f.parts = any ? a.B * pl.nc : 0;
-  hipLaunchKernelGGL((scan_bwd_finish_kernel<E>), dim3((unsigned)(f.bc + f.dA + f.dV + f.seam)),
-                     dim3(kScanFinThreads), 0, (hipStream_t)a.stream, p, f);
-  return hipGetLastError();
+  return launch_slices(f.bc + f.dA + f.dV + f.seam, kScanFinThreads,
+                       [&](uint32_t first, dim3 grid) {
+    p.first = first;
+    hipLaunchKernelGGL((scan_bwd_finish_kernel<E>), grid, dim3(kScanFinThreads), 0,
+                       (hipStream_t)a.stream, p, f);
+  });
 }
 
 hipError_t scan_bwd_launch(const ScanArgs &a) { return a.bf16 ? bwd<bf16>(a) : bwd<float>(a); }

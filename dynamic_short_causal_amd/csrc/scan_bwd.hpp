@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * NW) void scan_bwd_sums_kernel(ScanBwdP p) {
   __shared__ __align__(16) float s_dp[CUT ? TT : 1][kScanCh];
   __shared__ __align__(16) float s_bc[TT * BR];
   const ScanArgs &a = p.a;
-  const ScanWhere at = scan_where(a.G, p.dg, p.nblk, p.nc);
+  const ScanWhere at = scan_where(blockIdx.x + p.first, a.G, p.dg, p.nblk, p.nc);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t0 = at.chunk * p.tc, t1 = min((int)a.T, t0 + p.tc);
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64 * NW)
   __shared__ __align__(16) float s_bc[TT * BR];
   static_assert(TT > HALO && TT % 8 == 0, "the rows after a tile lie in one tile");
   const ScanArgs &a = p.a;
-  const ScanWhere at = scan_where(a.G, p.dg, p.nblk, p.nc);
+  const ScanWhere at = scan_where(blockIdx.x + p.first, a.G, p.dg, p.nblk, p.nc);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int T = (int)a.T;
@@ -526,7 +526,8 @@ __global__ __launch_bounds__(64 * NW)
     const int64_t tokn = (int64_t)at.b * T + t;
     // the tile's parts of dC and dB
     {
-      float *o = p.ws.dbc + ((int64_t)blockIdx.x % (a.G * p.nblk) * a.B * T + tokn) * (2 * Np);
+      const int64_t col = (int64_t)(blockIdx.x + p.first) % (a.G * p.nblk);
+      float *o = p.ws.dbc + (col * a.B * T + tokn) * (2 * Np);
       const int n = min(TT, t1 - t) * 2 * Np;
       for (int i = threadIdx.x; i < n; i += 64 * NW) o[i] = s_dbc[i / (2 * Np)][i % (2 * Np)];
     }
@@ -655,18 +656,25 @@ __global__ __launch_bounds__(64 * NW)
 template <typename E, int NS, int NW, int WM, bool PACKED>
 static hipError_t scan_bwd_run(const ScanBwdP &p, int64_t groups) {
   hipStream_t s = (hipStream_t)p.a.stream;
-  const dim3 grid((unsigned)groups), block(64 * NW);
-  if (p.nc > 1)
-    hipLaunchKernelGGL((scan_bwd_sums_kernel<E, NS, NW, WM, PACKED, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((scan_bwd_sums_kernel<E, NS, NW, WM, PACKED, false>), grid, block, 0, s, p);
-  const hipError_t e = hipGetLastError();
+  constexpr int TH = 64 * NW;
+  ScanBwdP q = p;
+  const hipError_t e = launch_slices(groups, TH, [&](uint32_t first, dim3 grid) {
+    q.first = first;
+    if (p.nc > 1)
+      hipLaunchKernelGGL((scan_bwd_sums_kernel<E, NS, NW, WM, PACKED, true>), grid, dim3(TH), 0,
+                         s, q);
+    else
+      hipLaunchKernelGGL((scan_bwd_sums_kernel<E, NS, NW, WM, PACKED, false>), grid, dim3(TH), 0,
+                         s, q);
+  });
   if (e != hipSuccess) return e;
-  if (p.a.N % NS)
-    hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, true>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return launch_slices(groups, TH, [&](uint32_t first, dim3 grid) {
+    q.first = first;
+    if (p.a.N % NS)
+      hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, true>), grid, dim3(TH), 0, s, q);
+    else
+      hipLaunchKernelGGL((scan_bwd_kernel<E, NS, NW, WM, PACKED, false>), grid, dim3(TH), 0, s, q);
+  });
 }
 
 template <typename E, int NS, int NW> hipError_t scan_bwd_nw(const ScanBwdP &p, int64_t groups) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "dsc_device.hpp"
+#include "grid_slices.hpp"
 #include "scan_launch.hpp"
 
 namespace dsc {
@@ -28,6 +29,7 @@ struct ScanP {
   ScanArgs a;
   float *hend, *sdt;
   int dg, nblk, nc, tc;
+  uint32_t first;  // the launch's first workgroup among all
 };
 
 // Workspace of a backward call, in floats.
@@ -44,6 +46,7 @@ struct ScanBwdP {
   ScanArgs a;
   ScanBwdWs ws;
   int dg, nblk, nc, tc, tiles;
+  uint32_t first;
 };
 
 // V consecutive floats of LDS, aligned to their size (16 bytes at most)
@@ -62,10 +65,9 @@ __device__ __forceinline__ void st_lds(float *p, const float (&o)[V]) {
 struct ScanWhere {
   int b, chunk, g, c0, nch;
 };
-__device__ __forceinline__ ScanWhere scan_where(int G, int dg, int nblk, int nc,
+__device__ __forceinline__ ScanWhere scan_where(unsigned id, int G, int dg, int nblk, int nc,
                                                 int ch = kScanCh) {
   ScanWhere w;
-  unsigned id = blockIdx.x;
   const unsigned per = (unsigned)(G * nblk);
   const unsigned col = id % per;
   id /= per;

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * scan_fwd_waves(GR))
   __shared__ __align__(16) float s_du[WV][TT + GT][CP];  // then the sums of C h
   __shared__ __align__(16) float s_bc[2][(TT + GT) * BR];
   const ScanArgs &a = p.a;
-  const ScanWhere at = scan_where(a.G, p.dg, p.nblk, p.nc, CB);
+  const ScanWhere at = scan_where(blockIdx.x + p.first, a.G, p.dg, p.nblk, p.nc, CB);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int T = (int)a.T;
@@ -359,14 +359,19 @@ __global__ __launch_bounds__(64 * scan_fwd_waves(GR))
 template <typename E, int NS, int GR, int WM>
 static hipError_t scan_fwd_run(const ScanP &p, int64_t groups) {
   hipStream_t s = (hipStream_t)p.a.stream;
-  const dim3 grid((unsigned)groups), block(ScanGeo<NS, GR>::TH);
+  constexpr int TH = ScanGeo<NS, GR>::TH;
+  ScanP q = p;
   if (p.nc > 1) {
-    hipLaunchKernelGGL((scan_fwd_kernel<E, NS, GR, WM, true>), grid, block, 0, s, p);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_slices(groups, TH, [&](uint32_t first, dim3 grid) {
+      q.first = first;
+      hipLaunchKernelGGL((scan_fwd_kernel<E, NS, GR, WM, true>), grid, dim3(TH), 0, s, q);
+    });
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((scan_fwd_kernel<E, NS, GR, WM, false>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return launch_slices(groups, TH, [&](uint32_t first, dim3 grid) {
+    q.first = first;
+    hipLaunchKernelGGL((scan_fwd_kernel<E, NS, GR, WM, false>), grid, dim3(TH), 0, s, q);
+  });
 }
 
 template <typename E, int NS, int GR>
