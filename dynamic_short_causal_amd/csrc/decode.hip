@@ -20,6 +20,7 @@
 // matrix cores, so the rank contraction runs on the vector ALUs.
 #include "dsc_device.hpp"
 #include "decode_launch.hpp"
+#include "grid_slices.hpp"
 
 namespace dsc {
 
@@ -162,6 +163,7 @@ __global__ __launch_bounds__(kDecThreads) void decode_state_kernel(
 template <typename E, int W, int GPV, int NB>
 static hipError_t launch_dec_lr(const DecArgs &a, int nvec, float rho) {
   const int64_t n = (a.B + NB - 1) / NB * nvec;
+  if (const hipError_t e = one_launch((n + kDecThreads - 1) / kDecThreads, kDecThreads); e != hipSuccess) return e;
   const unsigned grid = (unsigned)((n + kDecThreads - 1) / kDecThreads);
   hipLaunchKernelGGL((decode_lr_kernel<E, W, GPV, NB>), dim3(grid), dim3(kDecThreads), 0,
                      (hipStream_t)a.stream, (const E *)a.x, (const E *)a.z, (const E *)a.U,
@@ -185,6 +187,7 @@ static hipError_t launch_dec(const DecArgs &a) {
     return launch_dec_lr<E, W, GPV, (NT <= 32 ? 4 : 2)>(a, nvec, rho);
   }
   const int64_t n = a.B * nvec;
+  if (const hipError_t e = one_launch((n + kDecThreads - 1) / kDecThreads, kDecThreads); e != hipSuccess) return e;
   const unsigned grid = (unsigned)((n + kDecThreads - 1) / kDecThreads);
   hipLaunchKernelGGL((decode_hw_kernel<E, W, GPV>), dim3(grid), dim3(kDecThreads), 0,
                      (hipStream_t)a.stream, (const E *)a.x, (const E *)a.w, (E *)a.state,
@@ -232,6 +235,7 @@ static hipError_t launch_state(const DecArgs &a) {
   const int nvec = (int)(a.D / V);
   const int64_t n = a.B * S * nvec;
   if (n == 0) return hipSuccess;
+  if (const hipError_t e = one_launch((n + kDecThreads - 1) / kDecThreads, kDecThreads); e != hipSuccess) return e;
   const unsigned grid = (unsigned)((n + kDecThreads - 1) / kDecThreads);
   hipLaunchKernelGGL((decode_state_kernel<E>), dim3(grid), dim3(kDecThreads), 0,
                      (hipStream_t)a.stream, (const E *)a.x, (E *)a.state, a.B, a.T, a.D, S,

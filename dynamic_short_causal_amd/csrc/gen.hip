@@ -38,6 +38,7 @@
 // Token rows past the end and filter columns past G*W are read clamped to the
 // last valid row / column: they only feed w entries that are never used.
 #include "dsc_device.hpp"
+#include "grid_slices.hpp"
 #include "gen_launch.hpp"
 
 namespace dsc {
@@ -391,6 +392,7 @@ hipError_t launch_gen_nc(const GenArgs &a, int64_t N, int GW) {
   const int64_t ntt = (N + kGT - 1) / kGT;
   const int64_t nblocks = ntt * ncb;
   if (nblocks > INT32_MAX) return hipErrorInvalidValue;
+  if (const hipError_t e = one_launch(nblocks, kGenThreads); e != hipSuccess) return e;
   const int ngrp = gen_groups(ntt, ncb, NC, a.Dh);
   const float rho = a.residual ? 1.f : 0.f;
   hipStream_t s = (hipStream_t)a.stream;

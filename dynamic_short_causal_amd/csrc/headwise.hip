@@ -37,6 +37,7 @@
 // that are not cache-resident: 3 % faster forward, 9 % faster backward).
 #include "dsc_device.hpp"
 #include "dsc_launch.hpp"
+#include "grid_slices.hpp"
 
 namespace dsc {
 
@@ -636,6 +637,7 @@ static hipError_t launch_hw_tall(const HwArgs &a) {
     const int nchunk = (int)((a.T + Tl::FTW - 1) / Tl::FTW);
     const int ncol = (nvec + 63) / 64;
     const int64_t nblocks = (int64_t)a.B * ((nchunk + Tl::FNW - 1) / Tl::FNW) * ncol;
+    if (const hipError_t e = one_launch(nblocks, 64 * Tl::FNW); e != hipSuccess) return e;
     hipLaunchKernelGGL((hw_fwd_kernel<E, W, GPV, ACT, VL>), dim3((unsigned)nblocks),
                        dim3(64 * Tl::FNW), 0, s, (const E *)a.x, (const E *)a.w, a.pos,
                        (E *)a.y, (int)a.T, a.D, G, a.H, nvec, ncol, nchunk, rho);
@@ -645,6 +647,7 @@ static hipError_t launch_hw_tall(const HwArgs &a) {
     const int U = 64 / L * L;              // lanes of a wave in whole groups
     const int ncol = (nvec + U - 1) / U;
     const int64_t nblocks = (int64_t)a.B * ((nchunk + Tl::BNW - 1) / Tl::BNW) * ncol;
+    if (const hipError_t e = one_launch(nblocks, 64 * Tl::BNW); e != hipSuccess) return e;
     hipLaunchKernelGGL((hw_bwd_kernel<E, W, GPV, ACT, VL>), dim3((unsigned)nblocks),
                        dim3(64 * Tl::BNW), 0, s, (const E *)a.x, (const E *)a.w,
                        (const E *)a.dy, a.pos, (E *)a.dx, (E *)a.dw, (int)a.T, a.D, G, a.H,
@@ -665,6 +668,7 @@ static hipError_t launch_hw_long(const HwArgs &a) {
   if (!a.bwd) {
     const int nvb = (nvec + kLongThreads - 1) / kLongThreads;
     const int64_t nblocks = (int64_t)a.B * nchunk * nvb;
+    if (const hipError_t e = one_launch(nblocks, kLongThreads); e != hipSuccess) return e;
     hipLaunchKernelGGL((hw_fwd_long_kernel<E, W, GPV, ACT, VL>), dim3((unsigned)nblocks),
                        dim3(kLongThreads), 0, s, (const E *)a.x, (const E *)a.w, a.pos,
                        (E *)a.y, (int)a.T, a.D, G, a.H, nvec, nvb, TC, nchunk, rho);
@@ -674,6 +678,7 @@ static hipError_t launch_hw_long(const HwArgs &a) {
     const int per = U * (kLongThreads / 64);   // vectors per workgroup
     const int nvb = (nvec + per - 1) / per;
     const int64_t nblocks = (int64_t)a.B * nchunk * nvb;
+    if (const hipError_t e = one_launch(nblocks, kLongThreads); e != hipSuccess) return e;
     hipLaunchKernelGGL((hw_bwd_long_kernel<E, W, GPV, ACT, VL>), dim3((unsigned)nblocks),
                        dim3(kLongThreads), 0, s, (const E *)a.x, (const E *)a.w,
                        (const E *)a.dy, a.pos, (E *)a.dx, (E *)a.dw, (int)a.T, a.D, G, a.H,

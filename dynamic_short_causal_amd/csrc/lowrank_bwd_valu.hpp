@@ -304,6 +304,7 @@ static hipError_t launch_lr_bwd_valu(const LrArgs &a, float *dzp, float *dUp) {
   const LbPlan p = lr_bwd_valu_plan(a.B, a.T, a.D, W);
   const int64_t nblocks = a.B * p.nchunk * (int64_t)p.nvb;
   if (nblocks == 0) return hipSuccess;
+  if (const hipError_t e = one_launch(nblocks, p.bs); e != hipSuccess) return e;
   hipLaunchKernelGGL((lr_bwd_valu_kernel<W, ACT>), dim3((unsigned)nblocks), dim3(p.bs), 0,
                      (hipStream_t)a.stream, (const bf16 *)a.x, (const bf16 *)a.z,
                      (const bf16 *)a.U, (const bf16 *)a.dy, (bf16 *)a.dx, dzp, dUp, (int)a.T,

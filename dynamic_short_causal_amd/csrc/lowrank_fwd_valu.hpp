@@ -24,6 +24,7 @@
 // scalar loads; U's rank pairs of the lane's group stay in registers.
 #pragma once
 #include "dsc_device.hpp"
+#include "grid_slices.hpp"
 #include "lowrank_impl.hpp"
 
 namespace dsc {
@@ -183,6 +184,7 @@ static hipError_t launch_lr_fwd_valu(const LrArgs &a) {
   const int TC = kLvChunk, nchunk = (int)((a.T + TC - 1) / TC);
   const int64_t nblocks = a.B * nchunk * (int64_t)nvb;
   if (nblocks == 0) return hipSuccess;
+  if (const hipError_t e = one_launch(nblocks, bs); e != hipSuccess) return e;
   hipLaunchKernelGGL((lr_fwd_valu_kernel<W, ACT, VL>), dim3((unsigned)nblocks), dim3(bs), 0,
                      (hipStream_t)a.stream, (const bf16 *)a.x, (const bf16 *)a.z,
                      (const bf16 *)a.U, a.pos, (bf16 *)a.y, (int)a.T, (int)a.D, a.R, TC, nchunk,

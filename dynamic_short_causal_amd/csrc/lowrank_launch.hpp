@@ -22,6 +22,7 @@ static hipError_t launch_lr_fwd_mfma(const LrArgs &a) {
   const int nchunk = (int)((a.T + TC - 1) / TC);
   const int64_t nblocks = a.B * nchunk * (int64_t)ncb;
   if (nblocks == 0) return hipSuccess;
+  if (const hipError_t e = one_launch(nblocks, kLrThreads); e != hipSuccess) return e;
   constexpr int smem = LrFwdGeo<E, W, GPV>::bytes;
   hipLaunchKernelGGL((lr_fwd_kernel<E, W, GPV, ACT, VL, RB>), dim3((unsigned)nblocks),
                      dim3(kLrThreads), smem, s, (const E *)a.x, (const E *)a.z,
@@ -40,6 +41,7 @@ static hipError_t launch_lr_fwd_cl(const LrArgs &a) {
   const int nchunk = (int)((a.T + TC - 1) / TC);
   const int64_t nblocks = a.B * nchunk * (int64_t)ncb;
   if (nblocks == 0) return hipSuccess;
+  if (const hipError_t e = one_launch(nblocks, kClThreads); e != hipSuccess) return e;
   hipLaunchKernelGGL((lr_fwd_cl_kernel<W, ACT, kLrFwdClPrefetch>), dim3((unsigned)nblocks),
                      dim3(kClThreads), LrFwdClGeo<W>::bytes, (hipStream_t)a.stream,
                      (const bf16 *)a.x, (const bf16 *)a.z, (const bf16 *)a.U, (bf16 *)a.y,
@@ -74,6 +76,7 @@ static hipError_t launch_lr_bwd_cl(const LrArgs &a) {
   float *dzp = (float *)a.ws;
   float *dUp = (float *)((char *)a.ws + p.dz_part);
   const int64_t nblocks = a.B * p.nchunk * p.ncb;
+  if (const hipError_t e = one_launch(nblocks, kClThreads); e != hipSuccess) return e;
   if (nblocks > 0) {
     constexpr int smem = LrBwdClGeo<W>::bytes;
     const int64_t N = a.B * a.T;
@@ -101,6 +104,7 @@ static hipError_t launch_lr_bwd(const LrArgs &a) {
     float *dzp = (float *)a.ws;
     float *dUp = (float *)((char *)a.ws + p.dz_part);
     const int64_t nblocks = a.B * p.nchunk * p.ncb;
+    if (const hipError_t e = one_launch(nblocks, kLrThreads); e != hipSuccess) return e;
     for (int rb0 = 0; nblocks > 0 && rb0 < RB; ++rb0) {
       constexpr int smem = LrBwdGeo<E, W, GPV, RB>::bytes;
       hipLaunchKernelGGL((lr_bwd_kernel<E, W, GPV, VL, RB>), dim3((unsigned)nblocks),

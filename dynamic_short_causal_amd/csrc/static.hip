@@ -23,6 +23,7 @@
 // G * W per (sequence, chunk group) goes to the workspace, and a second kernel
 // adds the rows in ascending order, so dw is bitwise reproducible.
 #include "dsc_device.hpp"
+#include "grid_slices.hpp"
 #include "static_launch.hpp"
 
 namespace dsc {
@@ -384,6 +385,7 @@ static hipError_t launch_st(const StArgs &a) {
       const int nchunk = (int)((a.T + kStTallTW - 1) / kStTallTW);
       const int ncol = (nvec + 63) / 64;
       const int64_t nblocks = a.B * ((nchunk + kStTallNW - 1) / kStTallNW) * ncol;
+      if (const hipError_t e = one_launch(nblocks, 64 * kStTallNW); e != hipSuccess) return e;
       hipLaunchKernelGGL((st_fwd_tall_kernel<E, W, GPV, ACT>), dim3((unsigned)nblocks),
                          dim3(64 * kStTallNW), 0, s, (const E *)a.x, (const E *)a.w, (E *)a.y,
                          (int)a.T, a.D, a.H, nvec, ncol, nchunk, rho);
@@ -393,6 +395,7 @@ static hipError_t launch_st(const StArgs &a) {
     const int nchunk = (int)((a.T + tc - 1) / tc);
     const int nvb = (nvec + kStFwdThreads - 1) / kStFwdThreads;
     const int64_t nblocks = a.B * nchunk * nvb;
+    if (const hipError_t e = one_launch(nblocks, kStFwdThreads); e != hipSuccess) return e;
     hipLaunchKernelGGL((st_fwd_kernel<E, W, GPV, ACT>), dim3((unsigned)nblocks),
                        dim3(kStFwdThreads), 0, s, (const E *)a.x, (const E *)a.w, (E *)a.y,
                        (int)a.T, a.D, a.H, nvec, nvb, tc, nchunk, rho);
@@ -403,6 +406,7 @@ static hipError_t launch_st(const StArgs &a) {
     const int U = 64 / L * L;              // vectors per workgroup, whole groups
     const int nvb = (nvec + U - 1) / U;
     const int64_t nblocks = a.B * p.ncg * nvb;
+    if (const hipError_t e = one_launch(nblocks, kStBwdThreads); e != hipSuccess) return e;
     hipLaunchKernelGGL((st_bwd_kernel<E, W, GPV, ACT>), dim3((unsigned)nblocks),
                        dim3(kStBwdThreads), 0, s, (const E *)a.x, (const E *)a.w,
                        (const E *)a.dy, (E *)a.dx, (float *)a.ws, (int)a.T, a.D, a.H, nvec,
@@ -411,6 +415,7 @@ static hipError_t launch_st(const StArgs &a) {
     if (e != hipSuccess) return e;
   }
   const int64_t GW = G * a.W;
+  if (const hipError_t e = one_launch((GW + kStRedThreads - 1) / kStRedThreads, kStRedThreads); e != hipSuccess) return e;
   const unsigned rgrid = (unsigned)((GW + kStRedThreads - 1) / kStRedThreads);
   hipLaunchKernelGGL((st_reduce_kernel<E>), dim3(rgrid), dim3(kStRedThreads), 0, s,
                      (const float *)a.ws, (E *)a.dw, GW,

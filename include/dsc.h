@@ -56,7 +56,11 @@
  *   DSC_ERR_WORKSPACE    workspace smaller than dsc_lowrank_bwd_workspace_bytes
  *                        (dsc_static_bwd_workspace_bytes for dsc_static_bwd),
  *                        or NULL while that is non-zero;
- *   DSC_ERR_HIP          a HIP launch error (the message holds HIP's text).
+ *   DSC_ERR_HIP          a HIP launch error (the message holds HIP's text), or a
+ *                        convolution call of 2^32 threads or more, which one
+ *                        launch does not run (2^24 sequences of a few tokens
+ *                        and channels, for instance; the scan and layer norm
+ *                        take several launches).
  * B == 0 or T == 0 is legal and empty; the low-rank backward then still
  * writes dU = 0.
  */

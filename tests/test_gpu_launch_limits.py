@@ -101,3 +101,28 @@ def test_many_sequences_backward(dsc):
 def test_many_gradients_of_B_and_C(dsc):
     """The last launch has a thread for each element of dBm and dCm."""
     backward(dsc, (1 << 19) + 3, 64, 64)
+
+
+@pytest.mark.parametrize("name", ["headwise_fwd", "headwise_bwd", "static_fwd", "lowrank_fwd",
+                                  "lowrank_bwd", "decode_state"])
+def test_the_convolutions_refuse_what_one_launch_does_not_run(dsc, name):
+    """One workgroup a sequence of one token: they are not cut into launches, and
+    leave nothing unwritten without saying so."""
+    B, D = (1 << 24) + 1, 8
+    if name == "decode_state":
+        B = (1 << 32) // 7 + 1
+        x = torch.empty(B, 1, D, dtype=BF16, device=gu.dev())
+        with pytest.raises(dsc.DscError):
+            dsc.decode_state(x, 8)
+        return
+    x = torch.zeros(B, 1, D, dtype=BF16, device=gu.dev())
+    w = torch.zeros(B, 1, 1, 4, dtype=BF16, device=gu.dev())
+    z = torch.zeros(B, 1, 4, dtype=BF16, device=gu.dev())
+    U = torch.zeros(4, D * 4, dtype=BF16, device=gu.dev())
+    call = {"headwise_fwd": lambda: dsc.headwise_fwd(x, w, 8),
+            "headwise_bwd": lambda: dsc.headwise_bwd(x, w, x, 8),
+            "static_fwd": lambda: dsc.static_fwd(x, U.view(4 * D, 4)[:D].contiguous(), 1),
+            "lowrank_fwd": lambda: dsc.lowrank_fwd(x, z, U, 4, 1),
+            "lowrank_bwd": lambda: dsc.lowrank_bwd(x, z, U, x, 4, 1)}[name]
+    with pytest.raises(dsc.DscError):
+        call()
