@@ -32,8 +32,8 @@ EXPORTS = ("dsc_version", "dsc_status_string", "dsc_last_error", "dsc_headwise_f
            "dsc_static_bwd", "dsc_headwise_fwd_varlen", "dsc_headwise_bwd_varlen",
            "dsc_lowrank_fwd_varlen", "dsc_lowrank_bwd_varlen", "dsc_headwise_gen_fwd",
            "dsc_lowrank_bwd_noalloc", "dsc_scan_fwd_workspace_bytes", "dsc_scan_fwd",
-           "dsc_scan_bwd_workspace_bytes", "dsc_scan_bwd", "dsc_scan_decode", "dsc_layernorm_fwd", "dsc_layernorm_bwd_workspace_bytes",
-           "dsc_layernorm_bwd")
+           "dsc_scan_bwd_workspace_bytes", "dsc_scan_bwd", "dsc_scan_decode",
+           "dsc_layernorm_fwd", "dsc_layernorm_bwd_workspace_bytes", "dsc_layernorm_bwd")
 
 # bytes of the library-owned buffer behind dsc_lowrank_bwd_noalloc (include/dsc.h)
 NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -665,7 +665,9 @@ def scan_fwd(x, delta, A, Bm, Cm, w=None, cb=None, Dk=None, z=None, dt_bias=None
              conv0=None, pos=None, residual=False, act=False, final_state=False, workspace=None,
              stream=None):
     """y, or (y, hT, convT) with final_state: what scan_decode, or the next part
-    of a prompt (as h0 and conv0), goes on from."""
+    of a prompt (as h0 and conv0), goes on from.  With pos, convT holds the row's
+    last inputs whatever their document: before a scan_decode, clear those from
+    before a last document of fewer than W - 1 tokens."""
     B, T, D = x.shape
     N, W = A.shape[-1], 0 if w is None else w.shape[-1]
     if workspace is None:

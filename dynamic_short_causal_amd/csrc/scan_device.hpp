@@ -11,7 +11,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // log(1 + e^v) = max(v, 0) + log1p(e^-|v|), the logarithm as
 // 2 atanh(s), s = e / (2 + e) <= 1/3: atanh(s) / s as a polynomial in s^2,
-// fitted on [0, 1/9] for the smallest relative error (4e-9).  The result keeps
+// fitted on [0, 1/9] for the smallest relative error (8e-9).  The result keeps
 // single precision's relative error also where it is small.
 __device__ __forceinline__ float softplus_f(float v) {
   const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(v));

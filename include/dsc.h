@@ -290,7 +290,7 @@ dsc_status dsc_headwise_gen_fwd(const void *x, const void *xh, const void *Mt, v
  * any convolution that the caller has applied, the dynamic one for instance).
  * Per sequence b, channel c < D and state n < N, g(c) = floor(c / (D / G)):
  *
- *   s[t,c]   = cb[c] + sum_{k<W} w[c,k] x[t-k,c]       (W == 0: s = x)
+ *   s[t,c]   = cb[c] + sum_{k<W} w[c,k] x[t-k,c]       (W == 0: s = cb + x)
  *   u[t,c]   = act(s[t,c]) + rho x[t,c]
  *   dt[t,c]  = softplus(delta[t,c] + dt_bias[c])
  *   h[t,c,n] = exp(dt[t,c] A[c,n]) h[t-1,c,n] + dt[t,c] u[t,c] Bm[t,g(c),n]
@@ -336,7 +336,10 @@ size_t dsc_scan_fwd_workspace_bytes(const dsc_scan_shape *shape);
 
 /* Forward.  hT and convT receive the state after the last token and the last
  * W-1 inputs: what dsc_scan_decode, or the next part of a prompt (as h0 and
- * conv0, in other buffers), goes on from. */
+ * conv0, in other buffers), goes on from.  With pos, convT holds the last inputs
+ * of the row whatever their document: where the last document has fewer than W-1
+ * tokens, the next part's pos drops the older ones, but a decode step, which has
+ * no positions, would reach them; clear those rows of convT first. */
 dsc_status dsc_scan_fwd(const dsc_scan_shape *shape, const void *x, const void *delta,
                         const float *A, const void *Bm, const void *Cm, const void *w,
                         const void *cb, const float *Dk, const void *z, const float *dt_bias,
@@ -345,7 +348,8 @@ dsc_status dsc_scan_fwd(const dsc_scan_shape *shape, const void *x, const void *
                         void *stream);
 
 /* Bytes of workspace dsc_scan_bwd needs: the states at the starts of short runs
- * of tokens, and partial sums.  0 for arguments it would reject. */
+ * of tokens, and partial sums.  It depends on every size, W and the dtype
+ * included: ask with the shape of the call.  0 for arguments it would reject. */
 size_t dsc_scan_bwd_workspace_bytes(const dsc_scan_shape *shape);
 
 /*
