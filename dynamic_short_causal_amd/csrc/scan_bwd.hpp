@@ -32,7 +32,7 @@
 // other's barriers and LDS bound it: main issues 30 instructions a state
 // update, 20 of them in the two recurrences (the exponential of a step twice,
 // 4.5 for the sums over channels), and keeps the vector units 80 % busy.  8 x
-// 4096 x 1536, N = 16, bf16: 1.27 ms, of which sums 0.32, main 0.95 and the last
+// 4096 x 1536, N = 16, bf16: 1.28 ms, of which sums 0.32, main 0.95 and the last
 // launch 0.02; the 0.7 GB of tensors take 137 us.  Tiles of eight tokens would
 // allow three waves a SIMD, but store and read twice the states: 8 x 2048 x
 // 1536 bf16 790 us against 708.

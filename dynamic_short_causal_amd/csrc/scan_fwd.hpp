@@ -21,8 +21,10 @@
 // One state update is two products, two fused multiply-adds and an exponential,
 // 24.5 cycles of a SIMD's issue; the preparation, the exchange and the loop add
 // as much again.  The issue of vector instructions bounds the kernel: 16 x 4096
-// x 1536, N = 16, bf16 takes 580 us, of which the state updates' own
-// instructions are 251 us and the 0.8 GB moved 157 us.
+// x 1536, N = 16, bf16 takes 584 us, of which the state updates' own
+// instructions are 251 us and the 0.8 GB moved 157 us.  It issues 9.8 instructions
+// an update there, with two states a lane; with four, 8.7, but whole rows of that
+// size then leave the SIMDs unevenly filled (scan_plan).
 //
 // A call with few channels and a long axis cuts the axis into chunks: a first
 // launch (SUM) leaves the state that each chunk ends in when it starts from
